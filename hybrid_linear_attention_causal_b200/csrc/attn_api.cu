@@ -107,7 +107,8 @@ int attend(const Call& c) {
     a.ps_shift = log2_of(c.cfg->page_size);
     a.window = c.cfg->window;
     a.scale2 = (c.cfg->scale > 0.0f ? c.cfg->scale : 1.0f / sqrtf((float)D)) * gdn::attn::kLog2e;
-    a.cap2 = c.cfg->logit_cap > 0.0f ? c.cfg->logit_cap * gdn::attn::kLog2e : 0.0f;
+    // (a cap outside the limits makes every score zero, or changes none; within them nothing overflows in the kernels)
+    a.cap2 = c.cfg->logit_cap > 0.0f ? fminf(fmaxf(c.cfg->logit_cap * gdn::attn::kLog2e, 0x1p-100f), 0x1p120f) : 0.0f;
     a.q = c.q;
     a.q_stride = qs;
     a.cu = c.cu;

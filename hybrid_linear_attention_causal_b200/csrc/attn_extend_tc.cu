@@ -322,12 +322,12 @@ __device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
 
 // 16 scores scaled and capped.  (A polynomial tanh for scores below the cap, in place of two more visits to the unit
 // of the exponentials, was no faster.)
-template <bool F32> __device__ __forceinline__ void cap16(float* x, float a, float cap2, float cap_in) {
+template <Cap CAP> __device__ __forceinline__ void cap16(float* x, float a, float cap2, float cap_in) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = capped<F32>(x[i] * a, cap2, cap_in);
+    for (int i = 0; i < 16; ++i) x[i] = capped<CAP>(x[i] * a, cap2, cap_in);
 }
 
-template <typename T, int D, bool CAP>
+template <typename T, int D, Cap CAP>
 __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_constant__ Args p) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int kRows = item_rows<F32>();
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 // (every row sees the tokens up to pos_first: of a tree, not even the first draft)
                 const int pos_first = s.g.base + (p.parents ? -1 : p.token_of(r_first)), pos_last = s.g.base + p.token_of(r_last);
                 const float slope = p.slopes ? p.slopes[hq] * kLog2e : 0.0f;
-                const float cap2 = p.cap2, cap_in = CAP ? 2.0f * kLog2e / cap2 : 0.0f;
+                const float cap2 = p.cap2, cap_in = CAP != kNoCap ? 2.0f * kLog2e / cap2 : 0.0f;
 
                 for (int j = 0; j < nt && ok; ++j) {
                     const int i = s.twin ? 2 * j + st : j, k = k0 + i, t0 = (k < ta ? k : k + skip) * kTile, es = (tile + i) % kExpSlots;
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                         f.x = fmaxf(1.0e-37f, fminf(rs * f.x, 3.0e38f));  // a masked score, -inf, stays that
                         return f;
                     };
-                    const bool plain = !CAP && !p.slopes;  // scores are only scaled, below; otherwise the scale below is 1
+                    const bool plain = CAP == kNoCap && !p.slopes;  // scores are only scaled, below; otherwise the scale below is 1
                     if (!whole) {
                         // Mask (unless plain: scale, cap and bias too) in tensor memory, 16 columns at a time, in loops of
                         // their own: unrolled over the registers below they would double the loop's code.
@@ -607,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                                 tc::tmem_ld16(tS + g * 16, y);
                                 const float a = scale(g).x;
                                 tc::tmem_ld_wait();
-                                if constexpr (CAP) cap16<F32>(y, a, cap2, cap_in);
-                                if (!CAP && !plain)
+                                if constexpr (CAP != kNoCap) cap16<CAP>(y, a, cap2, cap_in);
+                                if (CAP == kNoCap && !plain)
 #pragma unroll
                                     for (int i = 0; i < 16; ++i) y[i] *= a;
                                 edit(y, t0 + g * 16);
@@ -648,10 +648,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 #pragma unroll
                     for (int c = 0; c < kTile; c += 32) tmem_ld32(tS + c, x + c);
                     tc::tmem_ld_wait();
-                    if constexpr (CAP) {  // scaled and capped here; below the scale is 1
+                    if constexpr (CAP != kNoCap) {  // scaled and capped here; below the scale is 1
                         if (whole)
 #pragma unroll
-                            for (int g = 0; g < kTile / 16; ++g) cap16<F32>(x + g * 16, scale(g).x, cap2, cap_in);
+                            for (int g = 0; g < kTile / 16; ++g) cap16<CAP>(x + g * 16, scale(g).x, cap2, cap_in);
                     }
                     float mx = -INFINITY;
 #pragma unroll
@@ -1059,7 +1059,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const __grid_constant__ 
     }
 }
 
-template <typename T, int D, bool CAP>
+template <typename T, int D, Cap CAP>
 cudaError_t launch(const Args& p, cudaStream_t s) {
     constexpr int kRows = item_rows<sizeof(T) == 4>();
     const int smem = (int)sizeof(Smem<D, kRows>);
@@ -1075,7 +1075,12 @@ cudaError_t launch(const Args& p, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t launch_dim(const Args& p, cudaStream_t s) {
-    return p.cap2 > 0.0f ? launch<T, D, true>(p, s) : launch<T, D, false>(p, s);
+    constexpr bool F32 = sizeof(T) == 4;
+    const Cap cap = cap_form<F32>(p.cap2);
+    if (cap == kNoCap) return launch<T, D, kNoCap>(p, s);
+    if constexpr (!F32)
+        if (cap == kExpCap) return launch<T, D, kExpCap>(p, s);
+    return launch<T, D, kTanhCap>(p, s);
 }
 
 size_t round16(size_t x) { return (x + 15) & ~(size_t)15; }

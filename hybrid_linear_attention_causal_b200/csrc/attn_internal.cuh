@@ -22,7 +22,7 @@ struct Args {
     int ps_shift;  // log2(page_size)
     int window;    // <= 0: none
     float scale2;  // scale * log2(e): scores are kept in base-2 units
-    float cap2;    // logit_cap * log2(e), 0: none
+    float cap2;    // logit_cap * log2(e) within 2^-100 .. 2^120, 0: none
     const void* q;
     long long q_stride;
     const int32_t* cu;       // [N+1], or null: `per` rows each
@@ -183,10 +183,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// cap * tanh(x / cap) in base-2 units: cap - 2 cap / (1 + e^(2 x / cap)), cap_in = 2 log2(e) / cap.  Its error
-// of about 2^-23 cap disappears in bf16 weights; fp32 takes the library's tanh.
-template <bool F32> __device__ __forceinline__ float capped(float x, float cap2, float cap_in) {
-    if constexpr (F32) return cap2 * tanhf(__fdividef(x, cap2));
+// The two forms of cap * tanh(x / cap), in base-2 units.  kExpCap: cap - 2 cap / (1 + e^(2 x / cap)), cap_in =
+// 2 log2(e) / cap; it is off by up to 2^-20 of the cap however small the score, so it serves bf16 alone, up to kMaxExpCap,
+// where that is less than the weights' rounding to fp16.  kTanhCap: the library's tanh, off by 2^-20 of the score
+// whatever the cap, for fp32 and for larger caps.  Caps 256 and 257 (B200): 12373 rows in a window, 16/4 heads of 128, 320
+// and 507 us; 32 rows per key (64 requests of 500 to 8000 tokens, 8 key heads) 196 and 256 us; 8 rows per key 95.5 and 96.6 us.
+enum Cap { kNoCap, kExpCap, kTanhCap };
+constexpr float kMaxExpCap = 256.0f * kLog2e;
+template <bool F32> inline Cap cap_form(float cap2) {
+    return !(cap2 > 0.0f) ? kNoCap : F32 || cap2 > kMaxExpCap ? kTanhCap : kExpCap;
+}
+template <Cap CAP> __device__ __forceinline__ float capped(float x, float cap2, float cap_in) {
+    if constexpr (CAP == kTanhCap) return cap2 * tanhf(__fdividef(x, cap2));
     else return cap2 - __fdividef(2.0f * cap2, 1.0f + tc::ex2_approx(x * cap_in));
 }
 

@@ -124,7 +124,7 @@ __device__ __forceinline__ Request get_request(const Args& p, int n, int rows_pe
     return q;
 }
 
-template <typename T, int D, int NB>
+template <typename T, int D, int NB, Cap CAP>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NB)) split_kernel(const __grid_constant__ Args p) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int kRows = 8 * NB;
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NB)) split_kernel(con
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float& x = s[j][i >> 1][2 * e + (i & 1)];
-                            if (p.cap2 > 0.0f) x = capped<F32>(x * a, p.cap2, cap_in) + (float)ve[j];
+                            if (p.cap2 > 0.0f) x = capped<CAP>(x * a, p.cap2, cap_in) + (float)ve[j];
                             else x = fmaf(x, a, (float)ve[j]);
                         }
                     }
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NB)) split_kernel(con
                             const float a = fminf(rs[i] * kf[j], 3.0e38f);
                             if (modified) {
                                 x *= a;
-                                if (p.cap2 > 0.0f) x = capped<F32>(x, p.cap2, cap_in);
+                                if (p.cap2 > 0.0f) x = capped<CAP>(x, p.cap2, cap_in);
                                 x = fmaf(-slope[i], fabsf((float)(pos[i] - at)), x) + (float)ve[j];
                             } else {
                                 x = fmaf(x, a, (float)ve[j]);  // as above: a mask changes no bit of what is seen
@@ -692,16 +692,25 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
     }
 }
 
-template <typename T, int D, int NB>
-cudaError_t launch_rows(const Args& p, cudaStream_t s) {
+template <typename T, int D, int NB, Cap CAP>
+cudaError_t launch_cap(const Args& p, cudaStream_t s) {
     const int smem = kWarps * (int)sizeof(WarpSmem<D, NB, sizeof(T) == 4>);
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(split_kernel<T, D, NB>), smem, done);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(split_kernel<T, D, NB, CAP>), smem, done);
     if (e != cudaSuccess) return e;
-    split_kernel<T, D, NB><<<grid_size(D, NB), kThreads, smem, s>>>(p);
+    split_kernel<T, D, NB, CAP><<<grid_size(D, NB), kThreads, smem, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_after(join_kernel<T, D>, dim3(kJoinGrid, 8 * NB), 128, 0, s, p, 8 * NB, num_workers(D, NB));
+}
+
+// CAP is the form of a cap if there is one: whether there is, the kernel asks for itself
+template <typename T, int D, int NB>
+cudaError_t launch_rows(const Args& p, cudaStream_t s) {
+    constexpr bool F32 = sizeof(T) == 4;
+    if constexpr (!F32)
+        if (cap_form<F32>(p.cap2) != kTanhCap) return launch_cap<T, D, NB, kExpCap>(p, s);
+    return launch_cap<T, D, NB, kTanhCap>(p, s);
 }
 
 template <typename T, int D>

@@ -39,6 +39,7 @@
  * fp16 (for fp32 a second fp16 takes their remainder), the output is rounded once to the dtype.  A token's
  * weight times its value page's scale keeps all those bits down to 2^-14 (fp32: 2^-26) of the largest such
  * product of its row; below that it is off by at most 2^-25 (2^-37) of that product.
+ * A capped score is off by at most 2^-20 of the score itself (bf16 with caps up to 256: 2^-20 of the cap).
  *
  * Conventions (as in gdn.h): every pointer is device memory owned by the caller and 16-byte aligned
  * (k_exp and v_exp: any alignment); calls are asynchronous and ordered on `stream`, allocate nothing and

@@ -77,9 +77,11 @@ def values(cache: dict, name: str, pages, h: int, count: int) -> np.ndarray:
 
 
 def attend(cache: dict, q, lens, kv_lens, table, page_size: int, scale: float = 0.0, cap: float = 0.0,
-           window: int = 0, slopes=None, prefix=None, parents=None):
+           window: int = 0, slopes=None, prefix=None, parents=None, faint: bool = False):
     """(out, lse, spread, reach) for packed rows q [T, HQ, D]; spread [T, HQ, D] = sum_j p_j |v_j| and reach
-    [T, HQ] = the largest scale * sum_d |q_d k_jd| over visible tokens, for error bounds."""
+    [T, HQ] = the largest scale * sum_d |q_d k_jd| over visible tokens, for error bounds.  With `faint` a fifth array
+    [T, HQ, D]: the sum of |code_jd| over visible tokens times the largest p_j 2^(value exponent of j) among them,
+    the scale of errors of weights that are small beside that."""
     q = np.asarray(q, dtype=np.float64)
     T, HQ, D = q.shape
     HKV = cache["k"].shape[1]
@@ -87,6 +89,7 @@ def attend(cache: dict, q, lens, kv_lens, table, page_size: int, scale: float = 
     scale = scale if scale > 0 else 1.0 / math.sqrt(D)
     out, spread = np.zeros((T, HQ, D)), np.zeros((T, HQ, D))
     lse, reach = np.full((T, HQ), -np.inf), np.zeros((T, HQ))
+    far = np.zeros((T, HQ, D))
     row0 = 0
     for n, L in enumerate(lens):
         kv = int(kv_lens[n])
@@ -119,6 +122,7 @@ def attend(cache: dict, q, lens, kv_lens, table, page_size: int, scale: float = 
         for h in range(HKV):
             K = np.where(live[:, None], values(cache, "k", pages, h, kv), 0.0)
             V = np.where(live[:, None], values(cache, "v", pages, h, kv), 0.0)
+            step = np.repeat(2.0 ** cache["v_exp"][pages, h].astype(np.float64), page_size)[:kv]
             for g in range(h * G, h * G + G):
                 x = q[row0:row0 + L, g]
                 s = scale * x @ K.T
@@ -134,7 +138,9 @@ def attend(cache: dict, q, lens, kv_lens, table, page_size: int, scale: float = 
                 p = w / np.where(l > 0, l, 1.0)
                 out[row0:row0 + L, g] = p @ V
                 spread[row0:row0 + L, g] = p @ np.abs(V)
+                if faint:
+                    far[row0:row0 + L, g] = (p * step).max(-1, keepdims=True) * (sees @ np.abs(V / step[:, None]))
                 lse[row0:row0 + L, g][some] = (m + np.log(np.where(l > 0, l, 1.0)))[some, 0]
                 reach[row0:row0 + L, g] = np.where(sees, scale * np.abs(x) @ np.abs(K).T, 0.0).max(-1)
         row0 += L
-    return out, lse, spread, reach
+    return (out, lse, spread, reach, far) if faint else (out, lse, spread, reach)
