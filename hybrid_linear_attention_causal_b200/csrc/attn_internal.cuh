@@ -94,9 +94,10 @@ template <bool F32> __host__ __device__ constexpr float lift() { return F32 ? 12
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
 // The exponent eq for which |x| <= amax times 2^-eq lies below 2^14 in fp16: a row of queries keeps all
-// of a bf16 value's bits down to 2^-28 of its largest.  The limits keep 2^-eq a normal number.
+// of a bf16 value's bits down to 2^-28 of its largest.  The lower limit keeps 2^-eq within exp2i's range (values below
+// 2^-113 need no more: bf16's smallest is 2^-133); the largest values need no limit (2^127: 114, inf: 115).
 __device__ __forceinline__ int query_exponent(float amax) {
-    return max(-100, min(100, (__float_as_int(amax) >> 23) - 127 - 13));  // amax >= 0; 0 and inf end at the limits
+    return max(-126, (__float_as_int(amax) >> 23) - 127 - 13);  // amax >= 0; inf: 115
 }
 
 template <typename T> struct Vec16;  // 16 bytes of a row

@@ -33,3 +33,15 @@ def test_caps_of_any_size(dtype, mode, D, hq, hkv, cap):
     c.q[0, 1] = 0.0
     attend(c, mode, D, dict(cap=cap), logit_cap=cap)
     attend(c, mode, D, dict(cap=cap, window=100, slopes=[0.1] * hq), logit_cap=cap, window=100, slopes=[0.1] * hq)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("mode,D", MODES)
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (60, 1)])
+@pytest.mark.parametrize("power", [123, 80, -80, -118])
+def test_queries_of_any_magnitude(dtype, mode, D, hq, hkv, power):
+    """Queries at both ends of their type's range, under a scale that brings the scores back to ordinary ones."""
+    c = Case(lens_of(mode, D, 3), [300, 20, 130], hq, hkv, 64 if hq == 4 else 128, 16, dtype, seed=52,
+             qscale=1.5 * 2.0 ** power)
+    scale = 0.1 * 2.0 ** -power
+    attend(c, mode, D, dict(scale=scale), scale=scale)
