@@ -57,3 +57,18 @@ def check_rows(c, got, **kw):
     none = np.isneginf(rlse)
     assert np.array_equal(np.isneginf(lse), none) and not out[none].any()
     assert np.all(np.abs(lse - rlse)[~none] <= ltol[~none])
+
+
+def extreme_case(make, lens, dtype, hq=4, hkv=2):
+    """Exponents far apart, queries of 1e4 and of 1e-20, pages of zeros; make: the class of the cases.  Only request
+    0 has the page of large values, so that request 1 shows what the other pages alone do."""
+    c = make(lens, [200, 150], hq, hkv, 128, 16, dtype, seed=9, elo=-12, ehi=-4)
+    c.np["v_exp"][c.table[0, 2]] = 20
+    c.np["v_exp"][c.table[0, 3]] = -32
+    c.np["v"][c.table[0, 3]] = 0
+    c.np["k_exp"][c.table[1, 1]] = -30
+    c.np["k"][c.table[1, 2]] = 0
+    c.q[0, 0] *= 1e4
+    c.q[0, 1] *= 1e-20
+    c.q[-1, 2] = 0.0
+    return c

@@ -3,7 +3,7 @@ and magnitudes far from the usual ones."""
 import pytest
 import torch
 
-from tests.attn_util import check_rows
+from tests.attn_util import check_rows, extreme_case
 from tests.test_gpu_attn import BF, F32, Case, call, random_tree
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +45,10 @@ def test_queries_of_any_magnitude(dtype, mode, D, hq, hkv, power):
              qscale=1.5 * 2.0 ** power)
     scale = 0.1 * 2.0 ** -power
     attend(c, mode, D, dict(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("mode,D", MODES)
+@pytest.mark.parametrize("hq", [4, 100])
+def test_exponents_far_apart(dtype, mode, D, hq):
+    attend(extreme_case(Case, lens_of(mode, D, 2), dtype, hq), mode, D)
