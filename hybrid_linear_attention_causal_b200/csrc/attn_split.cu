@@ -40,10 +40,17 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kSub = 32;                // tokens of a step
 constexpr int kStages = 2;
 constexpr int kItemSteps = 4;           // steps that beginning and ending an item takes the time of
-// NB: blocks of 8 rows (of an item) that share each widened code: 1, 2 or 4
-constexpr int ctas_per_sm(int D, int NB) { return NB == 1 ? (D == 64 ? 4 : 3) : D == 64 && NB == 2 ? 3 : 2; }
-constexpr int grid_size(int D, int NB) { return kSMs * ctas_per_sm(D, NB); }
-constexpr int num_workers(int D, int NB) { return grid_size(D, NB) * kWarps; }
+// NB: blocks of 8 rows (of an item) that share each widened code: 1, 2 or 4.
+// Blocks that an SM holds at a time, by registers and, for fp32's two parts of each query at D = 128, by shared memory
+// (the kernel asserts the latter): the list is cut for exactly the warps that run at once.  fp32 at D = 128 cut for bf16's
+// three blocks instead, of which two fit, had its last third wait for the rest: 64 requests of 64 to 16384 tokens, 32/8
+// heads, 110 us against 84; 4 of 100001 to 131072, 32/4 heads, 131 against 97.
+constexpr int ctas_per_sm(int D, int NB, bool F32) {
+    if (D == 128) return F32 ? (NB == 4 ? 1 : 2) : NB == 1 ? 3 : 2;
+    return NB == 1 ? 4 : NB == 2 ? 3 : 2;
+}
+constexpr int grid_size(int D, int NB, bool F32) { return kSMs * ctas_per_sm(D, NB, F32); }
+constexpr int num_workers(int D, int NB, bool F32) { return grid_size(D, NB, F32) * kWarps; }
 
 constexpr int kJoinGrid = 4 * kSMs;
 
@@ -125,13 +132,16 @@ __device__ __forceinline__ Request get_request(const Args& p, int n, int rows_pe
 }
 
 template <typename T, int D, int NB, Cap CAP>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NB)) split_kernel(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NB, sizeof(T) == 4)) split_kernel(const __grid_constant__ Args p) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int kRows = 8 * NB;
     constexpr int kDT = D / 16;  // row tiles of the output: dimensions
     using S = WarpSmem<D, NB, F32>;
     constexpr int kParts = F32 ? 2 : 1;
     extern __shared__ __align__(128) uint8_t smem_raw[];
+    // (beside the rings: s_sum below, and 1 KB that the system keeps)
+    static_assert(ctas_per_sm(D, NB, F32) * (kWarps * sizeof(S) + 1152 + 1024) <= 228 * 1024,
+                  "more blocks than an SM has shared memory for");
     const int lane = threadIdx.x & 31, worker = blockIdx.x * kWarps + (threadIdx.x >> 5), workers = gridDim.x * kWarps;
     S& sm = reinterpret_cast<S*>(smem_raw)[threadIdx.x >> 5];
     const int qr = lane >> 2, qc = lane & 3;  // fragment row (or column) and quad lane
@@ -637,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NB)) split_kernel(con
 // (i, r) handles row r of those of warps i, i + gridDim.x, ...
 template <typename T, int D>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args p, int rows_per_block, int workers) {
-    __shared__ float wts[num_workers(64, 1)];
+    __shared__ float wts[num_workers(64, 1, false)];  // the most of all forms
     __shared__ float red[8];
     __shared__ float acc[128 * 4];
     const int tid = threadIdx.x, r = blockIdx.y;
@@ -694,14 +704,16 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
 
 template <typename T, int D, int NB, Cap CAP>
 cudaError_t launch_cap(const Args& p, cudaStream_t s) {
-    const int smem = kWarps * (int)sizeof(WarpSmem<D, NB, sizeof(T) == 4>);
+    constexpr bool F32 = sizeof(T) == 4;
+    static_assert(num_workers(D, NB, F32) <= num_workers(64, 1, false), "the join holds a weight for each warp");
+    const int smem = kWarps * (int)sizeof(WarpSmem<D, NB, F32>);
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(split_kernel<T, D, NB, CAP>), smem, done);
     if (e != cudaSuccess) return e;
-    split_kernel<T, D, NB, CAP><<<grid_size(D, NB), kThreads, smem, s>>>(p);
+    split_kernel<T, D, NB, CAP><<<grid_size(D, NB, F32), kThreads, smem, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_after(join_kernel<T, D>, dim3(kJoinGrid, 8 * NB), 128, 0, s, p, 8 * NB, num_workers(D, NB));
+    return launch_after(join_kernel<T, D>, dim3(kJoinGrid, 8 * NB), 128, 0, s, p, 8 * NB, num_workers(D, NB, F32));
 }
 
 // CAP is the form of a cap if there is one: whether there is, the kernel asks for itself
@@ -728,7 +740,7 @@ struct Layout {
     explicit Layout(int D) {
         size_t warps = 0, rows = 0;
         for (int nr = 1; nr <= 4; nr *= 2) {
-            const size_t w = (size_t)num_workers(D, nr);
+            const size_t w = (size_t)num_workers(D, nr, false);  // bf16 has as many warps as fp32 or more
             warps = w > warps ? w : warps;
             rows = w * 8 * nr > rows ? w * 8 * nr : rows;
         }
