@@ -140,7 +140,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(const __grid_constant__ Args
     for (int n0 = 0; n0 < p.N; n0 += 1024) {
         const int n = n0 + tid;
         int nb = 0;
-        if (n < p.N) nb = ((p.cu ? p.cu[n + 1] - p.cu[n] : p.per) * p.G + item_rows - 1) / item_rows;
+        if (n < p.N) {
+            const int rows = (p.cu ? p.cu[n + 1] - p.cu[n] : p.per) * p.G;
+            nb = rows > p.rows_above ? (rows + item_rows - 1) / item_rows : 0;
+        }
         const long long at = scan(nb);
         if (n < p.N) {
             for (int i = 0; i < nb; ++i) p.items[at + i] = make_int2(n, i);

@@ -27,6 +27,7 @@ struct Args {
     long long q_stride;
     const int32_t* cu;       // [N+1], or null: `per` rows each
     int per, N, T;
+    int rows_above, rows_upto;  // the requests with rows_above < rows (per key/value head) <= rows_upto are this launch's
     const int32_t* kv_lens;  // [N]
     const int32_t* table;    // [N, max_pages]
     int max_pages;

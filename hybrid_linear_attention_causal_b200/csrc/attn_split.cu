@@ -116,7 +116,7 @@ __device__ __forceinline__ Request get_request(const Args& p, int n, int rows_pe
     q.bad_len = q.kv > 0 && (q.kv < q.L || (long long)q.kv > ((long long)p.max_pages << p.ps_shift));
     q.dead = q.kv <= 0 || q.bad_len;
     q.base = q.kv - q.L;
-    q.nb = (q.L * p.G + rows_per_block - 1) / rows_per_block;
+    q.nb = q.L * p.G <= p.rows_upto ? (q.L * p.G + rows_per_block - 1) / rows_per_block : 0;
     if (q.dead) {
         q.a = q.b = 0;
         q.tiles = 1;

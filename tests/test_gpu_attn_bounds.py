@@ -1,10 +1,12 @@
 """The 8-bit paged attention on the GPU within bounds taken row by row (tests/attn_util.py), at options, exponents
 and magnitudes far from the usual ones."""
+import numpy as np
 import pytest
 import torch
 
-from tests.attn_util import check_rows, extreme_case
-from tests.test_gpu_attn import BF, F32, Case, call, random_tree
+import hybrid_linear_attention_causal_b200 as gdn
+from tests.attn_util import bounds, check_rows, extreme_case
+from tests.test_gpu_attn import BF, F32, Case, call, i32, random_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +54,90 @@ def test_queries_of_any_magnitude(dtype, mode, D, hq, hkv, power):
 @pytest.mark.parametrize("hq", [4, 100])
 def test_exponents_far_apart(dtype, mode, D, hq):
     attend(extreme_case(Case, lens_of(mode, D, 2), dtype, hq), mode, D)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,L,hq,hkv", [(256, 2, 16, 2), (700, 2, 6, 2), (300, 8, 2, 2)])
+def test_short_extends_are_verified_drafts(dtype, n, L, hq, hkv):
+    """Many requests of few rows each: attn_extend and attn_verify take the same kernel, and give the same bits."""
+    rng = np.random.default_rng(53)
+    c = Case([L] * n, [int(x) for x in rng.integers(L, 150, n)], hq, hkv, 64, 32, dtype, seed=53)
+    got = call(c, "extend")
+    check_rows(c, got)
+    for a, b in zip(got, call(c, "verify", D=L)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("opts", [{}, dict(cap=20.0, window=70, slopes=[0.5 / (h + 1) for h in range(8)])])
+def test_long_requests_among_many_short_ones(dtype, opts):
+    """Requests on both sides of the rows at which the kernels change, with padding, lengths too short and too long,
+    requests without rows and rows behind the last request among them, on either side."""
+    rng = np.random.default_rng(54)
+    G, n = 4, 200
+    lens = [1] * n
+    for i, rows in ((3, 7), (50, 8), (51, 9), (52, 0), (90, 40), (91, 40), (92, 8), (120, 8), (150, 300), (199, 130)):
+        lens[i] = rows
+    kv = [int(max(l, x)) for l, x in zip(lens, rng.integers(1, 200, n))]
+    kv[150], kv[199], kv[60], kv[52] = 900, 130, 777, 30
+    c = Case(lens, kv, 2 * G, 2, 64, 16, dtype, seed=54)
+    T = sum(lens)
+    q = torch.cat([c.q, c.q[:9]]).cuda()
+    out = torch.full((T + 9, c.hq, c.d), 7.0, dtype=dtype, device="cuda")
+    names = dict(cap="logit_cap")
+    kw = {names.get(k, k): v for k, v in opts.items()}
+    got, lse = call(c, "extend", q=q, out=out.clone(), **kw)
+    check_rows(c, (got[:T], lse[:T]), **opts)
+    assert (got[T:] == 7.0).all() and torch.isnan(lse[T:]).all()
+    c.kv[90], c.kv[7] = -1, 0                   # padding: 160 rows per key, and 4
+    c.kv[91], c.kv[92] = 39, 7                  # shorter than their rows
+    c.kv[120] = c.mp * c.ps + 1                 # longer than the table
+    again, lagain = call(c, "extend", q=q, out=out, want_err=gdn.GDN_DEVERR_KV_LEN, **kw)
+    first = np.concatenate([[0], np.cumsum(lens)])
+    for i in (90, 7, 91, 92, 120):
+        rows = slice(first[i], first[i + 1])
+        assert not again[rows].any() and torch.isneginf(lagain[rows]).all()
+    keep = np.repeat([i not in (90, 7, 91, 92, 120) for i in range(n)], lens)
+    c.kv = [-1 if i in (91, 92, 120) else x for i, x in enumerate(c.kv)]
+    check_rows(c, (again[:T], lagain[:T]), **opts)
+    assert keep.sum() == T - 97
+
+
+def test_a_mixed_batch_captured():
+    """A captured extend whose lengths change place: the long request becomes short, and a short one long."""
+    lens = [[600, *[1] * 99], [*[1] * 70, 590, *[1] * 20, 10, *[0] * 8]]
+    cases = [Case(x, [max(y, 1) + 40 for y in x], 8, 2, 64, 16, BF, seed=55, extra_pages=3) for x in lens]
+    T = max(sum(x) for x in lens)
+    cfg = cases[0].cfg()
+    ws = gdn.alloc_workspace(gdn.attn_extend_workspace_size(cfg, 100, T), "cuda")
+    pages = max(c.np["k"].shape[0] for c in cases)
+    cache = gdn.alloc_attn_cache(cfg, pages, "cuda")
+    mp = max(c.mp for c in cases)
+    q, out = (torch.zeros((T, 8, 64), dtype=BF, device="cuda") for _ in range(2))
+    cu, kv, table = (torch.zeros(x, dtype=torch.int32, device="cuda") for x in ((101,), (100,), (100, mp)))
+    run = lambda: gdn.attn_extend(cfg, q, cu, kv, table, cache, out, ws)
+
+    def load(c):
+        t = sum(c.lens)
+        q[:t].copy_(c.q)
+        cu.copy_(i32(np.concatenate([[0], np.cumsum(c.lens)])))
+        kv.copy_(i32(c.kv))
+        table[:, :c.mp].copy_(torch.from_numpy(c.table))
+        for name in ("k", "v", "k_exp", "v_exp"):
+            x = torch.from_numpy(c.np[name])
+            getattr(cache, name)[:x.shape[0]].copy_(x)
+
+    load(cases[0])
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for c in (cases[1], cases[0]):
+        load(c)
+        g.replay()
+        torch.cuda.synchronize()
+        assert gdn.gdn_get_device_error(ws) == 0
+        ref, _, tol, _ = bounds(c)
+        got = out[:sum(c.lens)].cpu().double().numpy()
+        assert (np.abs(got - ref) <= tol).all()
