@@ -114,8 +114,11 @@ GDN_API size_t attn_append_workspace_size(const attn_config_t* cfg, int32_t max_
  * A page whose first token is written takes the smallest exponent e with amax <= 448 * 2^e over its new
  * rows.  A page that already holds tokens before the first new one keeps or raises its exponent, and when
  * it is raised those tokens' codes are rounded again to the nearest even code of the same value.  Tokens
- * from start + rows on are dropped (their rows keep stale codes), so a rejected draft is undone by
- * appending at its position.  Two requests that write the same page race; full pages may be shared.
+ * from start + rows on are dropped (their rows keep stale codes), so a rejected draft is replaced by
+ * appending at its position.  What it did to the page it began in stays, if tokens before it are there: an exponent
+ * that it raised, and those tokens' values, which that exponent's smallest step, 2^(exp - 9), moved by up to half of
+ * it.  (To be free of that, begin drafts on a page of their own, or append the page again from its first token.)
+ * Two requests that write the same page race; full pages may be shared.
  */
 GDN_API int attn_append(const attn_config_t* cfg, const attn_cache_t* cache, const void* k_new, const void* v_new,
                         int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens, int32_t N, int32_t T,

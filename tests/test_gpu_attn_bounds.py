@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import hybrid_linear_attention_causal_b200 as gdn
+from oracle import attn as A
 from tests.attn_util import bounds, check_rows, extreme_case
 from tests.test_gpu_attn import BF, F32, Case, call, i32, random_tree
 
@@ -141,3 +142,41 @@ def test_a_mixed_batch_captured():
         ref, _, tol, _ = bounds(c)
         got = out[:sum(c.lens)].cpu().double().numpy()
         assert (np.abs(got - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_what_a_rejected_draft_leaves(dtype):
+    """Outliers appended as drafts and replaced: the exponent they raised stays, earlier tokens of their page are off by up to
+    half its smallest step, pages before and after are as if the drafts had never been, and so is the page once it is
+    appended again from its first token."""
+    rng = np.random.default_rng(56)
+    ps, hkv, d = 16, 2, 64
+    cfg = gdn.AttnConfig(hkv, hkv, d, page_size=ps, dtype=dtype)
+    ws = gdn.alloc_workspace(gdn.attn_append_workspace_size(cfg, 1, 40), "cuda")
+    table = i32([[3, 0, 2, 1]])
+    x = torch.from_numpy(rng.standard_normal((40, hkv, d))).to(dtype)
+
+    def put(cache, rows, start):
+        gdn.attn_append(cfg, cache, rows.cuda(), rows.cuda(), None, i32([start]), table, ws)
+
+    caches = [gdn.alloc_attn_cache(cfg, 4, "cuda") for _ in range(2)]
+    for i, cache in enumerate(caches):
+        put(cache, x[:21], 0)
+        if i:
+            put(cache, x[21:33] * 1e4, 21)  # the drafts: pages 1 and 2 of the request
+        put(cache, x[21:40], 21)
+    torch.cuda.synchronize()
+    clean, after = ({n: getattr(c, n).cpu().numpy() for n in ("k", "v", "k_exp", "v_exp")} for c in caches)
+    assert gdn.gdn_get_device_error(ws) == 0
+    for n in "kv":
+        assert np.array_equal(clean[n][[3, 2]], after[n][[3, 2]])
+        assert np.array_equal(clean[n + "_exp"][[3, 2]], after[n + "_exp"][[3, 2]])
+        e = after[n + "_exp"][0].astype(float)
+        assert (e > clean[n + "_exp"][0]).all()
+        old, new = (A.CODE[c[n][0, :, :5]] * 2.0 ** c[n + "_exp"][0].astype(float)[:, None, None] for c in (clean, after))
+        assert (np.abs(new - old) <= 2.0 ** (e[:, None, None] - 10)).all() and (new != old).any()
+    put(caches[1], x[16:40], 16)
+    put(caches[0], x[16:40], 16)
+    torch.cuda.synchronize()
+    for n in ("k", "v", "k_exp", "v_exp"):
+        assert torch.equal(*(getattr(c, n) for c in caches))
