@@ -50,7 +50,8 @@
  *   - A request with kv_lens[n] < 0 (attn_append: start_lens[n] < 0) is padding: its output rows are
  *     zeros (lse -inf), nothing is appended for it.  kv_lens[n] == 0: the same.
  *   - kv_lens[n] (attn_append: start + rows) above max_pages * page_size, or below the request's row
- *     count, raises GDN_DEVERR_KV_LEN and the request is treated as padding.
+ *     count, raises GDN_DEVERR_KV_LEN and the request is treated as padding.  (Of a request without rows no length is
+ *     looked at: it may be a finished one's.)
  *   - A needed block_table entry outside 0 .. num_pages-1 raises GDN_DEVERR_PAGE_RANGE; its tokens are
  *     not read (attn_append: not written), and that request's outputs are invalid.
  *   - cu_seqlens must start at 0, not decrease, and end at or before T; otherwise GDN_DEVERR_SEQLENS is

@@ -7,7 +7,7 @@ import torch
 import hybrid_linear_attention_causal_b200 as gdn
 from oracle import attn as A
 from tests.attn_util import bounds, check_rows, extreme_case
-from tests.test_gpu_attn import BF, F32, Case, call, i32, random_tree
+from tests.test_gpu_attn import BF, F32, Case, call, fresh, gpu_append, i32, random_tree, same_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -180,3 +180,22 @@ def test_what_a_rejected_draft_leaves(dtype):
     torch.cuda.synchronize()
     for n in ("k", "v", "k_exp", "v_exp"):
         assert torch.equal(*(getattr(c, n) for c in caches))
+
+
+@pytest.mark.parametrize("hq", [4, 40])
+def test_lengths_of_requests_without_rows(hq):
+    """They raise nothing, wherever they point, in any call; the same lengths with a row do."""
+    c = Case([2, 0, 3, 0], [20, 30, 40, 50], hq, 2, 64, 16, BF, seed=57)
+    good = call(c, "extend")
+    c.kv[1], c.kv[3] = 16 * c.mp + 1, 2 ** 31 - 1
+    for a, b in zip(call(c, "extend"), good):
+        assert torch.equal(a, b)
+    c.kv[2] = 16 * c.mp + 1
+    call(c, "extend", want_err=gdn.GDN_DEVERR_KV_LEN)
+    rng = np.random.default_rng(57)
+    ref = fresh(4, 2, 16, 64, rng)
+    cache = gdn.AttnCache(**{n: torch.from_numpy(x.copy()).cuda() for n, x in ref.items()})
+    x = torch.from_numpy(rng.standard_normal((2, 2, 64))).to(BF)
+    gpu_append(x.cuda(), x.cuda(), [0, 0, 2], [2 ** 31 - 1, 5], [[0], [3]], cache, BF, 16, 2, 64)
+    A.append(ref, x.double().numpy(), x.double().numpy(), [0, 2], [0, 5], [[0], [3]], 16)
+    same_cache(cache, ref)
