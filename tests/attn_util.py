@@ -9,8 +9,11 @@ scale * sum_d |q_d k_jd| times log2(e), and n the tokens cached for its request:
   - the products add up in fp32, each addition off by at most 2^-22 of what it holds (the tensor core truncates): at most
     n / 16 + 8 additions (fp32: twice the products, 2 n / 16 + 16), of A each;
   - a score: its products in fp32 over at most 16 additions, 2^-18 R; queries in two fp16 for fp32, 2^-22 R; its own
-    steps and the base-2 exponential, 2^-21 R + 2 * 2^-22 R + 2^-21.  A score that is off by d changes a weight by
-    d ln2 of itself and the sum of weights likewise: 2 ln2 d A;
+    steps and the base-2 exponential, 2^-21 R + 2 * 2^-22 R + 2^-21; it is kept with its page's value exponent, at most E in
+    size, added, one rounding: 2^-24 (R + E).  A score that is off by d changes a weight by d ln2 of itself and the
+    sum of weights likewise: 2 ln2 d A;
+  - lse is the reference m, the largest score with its exponent less 12 at most, plus the logarithm of the sum: a score's
+    error, and three roundings of numbers up to R + E + 12 (the score, m, their sum): 3 ln2 2^-24 (R + E + 12);
   - a cap: up to 256 as cap - 2 cap / (1 + e), e = 2^(2 log2(e) s / cap): the division is off by 2^-22 of up to twice the
     cap, the exponential's 2^-22 comes through e / (1 + e)^2 <= 1/4 of that, the sums beside them add 3 * 2^-24 of the
     cap: below 2^-20 cap log2(e).  Above 256 (fp32: always) as cap * tanh(s / cap), whose division, tanh and product are off
@@ -33,7 +36,8 @@ def bounds(c, scale=0.0, cap=0.0, window=0, slopes=None, prefix=None, parents=No
                                               slopes, prefix, parents, faint=True)
     n = np.repeat(np.maximum(c.kv, 1), c.lens).astype(np.float64)[:, None]
     R = reach * math.log2(math.e)
-    d = R * (2.0 ** -18 + 2.0 ** -21 + 3 * 2.0 ** -22) + 2.0 ** -21
+    E = float(np.abs(c.np["v_exp"].astype(int)).max())
+    d = R * (2.0 ** -18 + 2.0 ** -21 + 3 * 2.0 ** -22) + 2.0 ** -21 + 2.0 ** -24 * (R + E)
     if cap:
         d = d + (R * 2.0 ** -20 if f32 or cap > 256.0 else cap * math.log2(math.e) * 2.0 ** -20)
     if slopes is not None:  # the bias is a product and a sum in fp32, of values up to n * slope
@@ -43,7 +47,8 @@ def bounds(c, scale=0.0, cap=0.0, window=0, slopes=None, prefix=None, parents=No
     tol = (2.0 ** -24 if f32 else 2.0 ** -8) * np.abs(out) + spread * rel[..., None] \
         + faint * 2.0 ** (-37 if f32 else -25) + 1e-30
     some = np.isfinite(lse)
-    ltol = np.where(some, d * math.log(2) + 2.0 ** -21 * (1 + np.abs(np.where(some, lse, 0.0))), 0.0)
+    ltol = np.where(some, math.log(2) * (d + 3 * 2.0 ** -24 * (R + E + 12)) + 2.0 ** -21 * (1 + np.abs(np.where(some, lse, 0.0))),
+                    0.0)
     return out, lse, tol, ltol
 
 
