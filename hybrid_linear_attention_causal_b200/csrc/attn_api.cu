@@ -105,7 +105,7 @@ int attend(const Call& c) {
     if (qs < 0) return GDN_ERR_INVALID_ARG;
     if ((int64_t)c.max_pages * c.cfg->page_size > (1 << 30)) return GDN_ERR_UNSUPPORTED;
     const int G = c.cfg->num_q_heads / c.cfg->num_kv_heads;
-    if ((int64_t)c.T * G >= (1 << 25)) return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)c.T * G >= (1 << 25) || c.N > (1 << 28)) return GDN_ERR_UNSUPPORTED;
     if (c.ws_bytes < c.ws_need) return GDN_ERR_WORKSPACE;
 
     gdn::attn::Args a{};

@@ -60,7 +60,7 @@
  * Rows of q, k_new and v_new may be further apart than their heads need (slices of a fused projection):
  * the *_stride arguments give the distance between rows in elements, 0 for contiguous rows; a row's
  * byte distance must be a multiple of 16.  out is contiguous [T, HQ, head_dim].  T * (HQ / HKV) must be below
- * 2^25 and max_pages * page_size at most 2^30 (GDN_ERR_UNSUPPORTED).
+ * 2^25 (attn_append: T at most 2^30), max_pages * page_size at most 2^30 and N at most 2^28 (GDN_ERR_UNSUPPORTED).
  */
 #ifndef ATTN_H
 #define ATTN_H
