@@ -464,7 +464,8 @@ class AttnConfig:
 @dataclass(frozen=True)
 class AttnCache:
     """The pools of a paged 8-bit cache: k, v [pages, HKV, page_size, head_dim] (uint8 or float8_e4m3fn codes),
-    k_exp, v_exp [pages, HKV] int8 (see include/attn.h).  The tensors are checked once, here."""
+    k_exp, v_exp [pages, HKV] int8 (see include/attn.h).  The tensors are checked here, and anew when their places or
+    k's shape change."""
     k: torch.Tensor
     v: torch.Tensor
     k_exp: torch.Tensor
@@ -482,10 +483,12 @@ class AttnCache:
             raise ValueError("cache: k_exp and v_exp are int8 exponents [pages, HKV] on the codes' device")
 
     def c(self) -> AttnCacheC:
-        at = (self.k.data_ptr(), self.v.data_ptr(), self.k_exp.data_ptr(), self.v_exp.data_ptr())
-        last = self.__dict__.get("_last")  # the struct of the call before, while the tensors lie where they lay
+        k = self.k
+        at = (k.data_ptr(), self.v.data_ptr(), self.k_exp.data_ptr(), self.v_exp.data_ptr(), k.shape)
+        last = self.__dict__.get("_last")  # the struct of the call before, while the tensors are what they were
         if last is None or last[0] != at:
-            last = (at, AttnCacheC(*at, self.k.shape[0]))
+            self.__post_init__()
+            last = (at, AttnCacheC(*at[:4], k.shape[0]))
             self.__dict__["_last"] = last
         return last[1]
 
