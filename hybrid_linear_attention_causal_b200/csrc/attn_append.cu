@@ -29,28 +29,12 @@ __device__ __forceinline__ uint32_t narrow2(float x0, float x1) {
     return r;
 }
 
-template <typename T> struct Vec;  // one 16-byte load
-template <> struct Vec<float> {
-    static constexpr int kN = 4;
-    static __device__ __forceinline__ void get(uint4 w, float* x) {
-        x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
-    }
-};
-template <> struct Vec<__nv_bfloat16> {
-    static constexpr int kN = 8;
-    static __device__ __forceinline__ void get(uint4 w, float* x) {
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(v[i] << 16), x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-    }
-};
-
 // Block (i, 2 h + keys or values).  With cu_seqlens, request n owns blocks f(n) .. f(n+1)-1, where
 // f(n) = cu[n] / ps + 2 n: at least as many as the pages that its rows can touch, without a scan.
 // NV: 16-byte vectors per thread that hold a page of rows.
 template <typename T, int D, int NV, int NT>
 __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ AppendArgs p) {
-    constexpr int kN = Vec<T>::kN, kPerRow = D / kN;  // vectors of a row
+    constexpr int kN = Vec16<T>::kN, kPerRow = D / kN;  // vectors of a row
     __shared__ int s_n, s_row0, s_len, s_start;
     __shared__ float s_max[NT / 32];
     __shared__ int s_bad;
@@ -124,7 +108,7 @@ __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ Appe
     for (int i = 0; i < NV; ++i)
         if ((i * NT + tid) / kPerRow < count) {
             float x[kN];
-            Vec<T>::get(w[i], x);
+            Vec16<T>::get(w[i], x);
 #pragma unroll
             for (int j = 0; j < kN; ++j) {
                 const float a = fabsf(x[j]);
@@ -148,7 +132,7 @@ __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ Appe
         const int e = i * NT + tid, r = e / kPerRow;
         if (r < count) {
             float x[kN];
-            Vec<T>::get(w[i], x);
+            Vec16<T>::get(w[i], x);
 #pragma unroll
             for (int j = 0; j < kN; ++j) x[j] = isnan(x[j]) ? 0.0f : x[j] * f;
             uint8_t* at = dst + (r0 + r) * D + (e % kPerRow) * kN;

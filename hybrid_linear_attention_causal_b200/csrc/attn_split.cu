@@ -351,24 +351,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NB, sizeof(T) == 4)) 
             if (r < rows) {
                 const int t = p.token_of(rr), hq = h * p.G + rr - t * p.G;
                 const T* src = static_cast<const T*>(p.q) + (long long)(rq.row0 + t) * p.q_stride + hq * D + c * 16;
-                if constexpr (F32) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 f = reinterpret_cast<const float4*>(src)[i];
-                        x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 w = reinterpret_cast<const uint4*>(src)[i];
-                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            x[8 * i + 2 * j] = __uint_as_float(ww[j] << 16);
-                            x[8 * i + 2 * j + 1] = __uint_as_float(ww[j] & 0xffff0000u);
-                        }
-                    }
-                }
+                for (int i = 0; i < 16; i += Vec16<T>::kN) Vec16<T>::get(*reinterpret_cast<const uint4*>(src + i), x + i);
             } else {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = 0.0f;
