@@ -52,6 +52,12 @@ constexpr int ctas_per_sm(int D, int NB, bool F32) {
 constexpr int grid_size(int D, int NB, bool F32) { return kSMs * ctas_per_sm(D, NB, F32); }
 constexpr int num_workers(int D, int NB, bool F32) { return grid_size(D, NB, F32) * kWarps; }
 
+// Steps that the tensor core adds up at a time.  Its additions truncate, so that a long sum shrinks, by some 2^-25 of itself
+// an addition (64 requests of 131072 tokens, 8 heads of 128: 1.4e-4 in fp32, of 1048576: 1.2e-3): what it holds is added to the
+// warp's partial result in fp32 instructions every 512 tokens for fp32 (64 additions; 9e-7 for either) and every 4096 for
+// bf16 (256; 6e-5).  Time: bf16 0 to 2 %, fp32 5 % (10 % with 32 rows per key).
+template <bool F32> constexpr int fold_steps() { return F32 ? 16 : 128; }
+
 constexpr int kJoinGrid = 4 * kSMs;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -86,6 +92,7 @@ template <int D, int NB, bool F32> struct alignas(128) WarpSmem {
     uint8_t ring[kStages][2][kTile];
     uint32_t q[F32 ? 2 : 1][NB][D / 64][4][32][2];  // B fragments of the queries (high, low fp16 parts)
     float rs[8 * NB];                               // scale2 * 2^eq of each row
+    float m_fold[8 * NB];                           // the reference of each row when its sums were last set aside
     int8_t exps[kStages][2][2];  // key and value exponents of a tile's two 16-token halves
     uint16_t anc[kMaxVerifyDraft];
     int8_t depth[kMaxVerifyDraft];
@@ -136,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NB, sizeof(T) == 4)) 
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int kRows = 8 * NB;
     constexpr int kDT = D / 16;  // row tiles of the output: dimensions
+    constexpr int kFold = fold_steps<F32>();
     using S = WarpSmem<D, NB, F32>;
     constexpr int kParts = F32 ? 2 : 1;
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -410,187 +418,225 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NB, sizeof(T) == 4)) 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nb][d][e] = 0.0f;
 
-        for (int it = 0; it < steps; ++it) {
-            copy_wait<kStages - 2>();
-            store_exp();
-            __syncwarp();  // the entry has landed for every lane, and the one before it has been read by all
-            fetch(it + kStages - 1);
-
-            const int st = it % kStages, t0 = tile_tok(it);
-            const uint8_t* ks = sm.ring[st][0];
-            const uint8_t* vs = sm.ring[st][1];
-            const float kf[2] = {exp2i(sm.exps[st][0][0]), exp2i(sm.exps[st][0][1])};
-            const int ve[2] = {sm.exps[st][1][0], sm.exps[st][1][1]};
-
-            // S^T[16 tokens][block of rows]: element e is token 16 j + 8 (e / 2) + qr, row 2 qc + e % 2
-            float s[2][NB][4];
+        // Adds the lane's sums, dim(d) and the seven dimensions behind it for d = 0, 4, .., to what has been set aside of the item, if
+        // anything: there (keep) or in the registers.
+        auto slot_of = [&] { return (long long)(worker * 2 + (k0 == 0 ? 1 : 0)) * kRows; };
+        auto fold = [&](bool any, bool keep) {
+            int first = (int)slot_of() + 2 * qc;
+            asm volatile("" : "+r"(first));  // formed here, not kept in registers through the steps
+            float* const mine = p.part_o + (long long)first * D + qr * (D / 8);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int i = 0; i < NR; ++i) {
+                const int r = 8 * (i >> 1) + 2 * qc + (i & 1);
+                const float mf = any ? sm.m_fold[r] : 0.0f, f = mf == -INFINITY ? 0.0f : tc::ex2_approx(mf - m[i]);
+                float4* at = reinterpret_cast<float4*>(mine + (8 * (i >> 1) + (i & 1)) * D);  // 4 dimensions each
+                float4 y[kDT / 2];
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
+                for (int d = 0; d < kDT / 2; ++d) y[d] = any ? at[d] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[j][nb][e] = 0.0f;
-#pragma unroll
-            for (int hh = 0; hh < D / 64; ++hh) {
-                uint32_t kw[4][4];  // rows 8 j + qr
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(ks + chunk_off<D>(8 * j + qr, qc + 4 * hh));
-                    kw[j][0] = w.x, kw[j][1] = w.y, kw[j][2] = w.z, kw[j][3] = w.w;
-                }
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    uint2 b[kParts][NB];
-#pragma unroll
-                    for (int part = 0; part < kParts; ++part)
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-                            b[part][nb] = *reinterpret_cast<const uint2*>(sm.q[part][nb][hh][kk][lane]);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t w0 = kw[2 * j][kk], w1 = kw[2 * j + 1][kk];
-                        const uint32_t a[4] = {widen_lo(w0), widen_lo(w1), widen_hi(w0), widen_hi(w1)};
-#pragma unroll
-                        for (int part = 0; part < kParts; ++part)
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) mma16816(s[j][nb], a, b[part][nb].x, b[part][nb].y);
+                for (int d = 0; d < kDT / 2; ++d) {
+                    float& x0 = o[i >> 1][2 * d][i & 1];
+                    float& x1 = o[i >> 1][2 * d][2 + (i & 1)];
+                    float& x2 = o[i >> 1][2 * d + 1][i & 1];
+                    float& x3 = o[i >> 1][2 * d + 1][2 + (i & 1)];
+                    x0 = fmaf(y[d].x, f, x0), x1 = fmaf(y[d].y, f, x1), x2 = fmaf(y[d].z, f, x2), x3 = fmaf(y[d].w, f, x3);
+                    if (keep) {
+                        at[d] = make_float4(x0, x1, x2, x3);
+                        x0 = x1 = x2 = x3 = 0.0f;
                     }
                 }
             }
+            __syncwarp();
+            if (keep && qr == 0)
+#pragma unroll
+                for (int i = 0; i < NR; ++i) sm.m_fold[8 * (i >> 1) + 2 * qc + (i & 1)] = m[i];
+        };
 
-            // scores in base-2 units plus the value exponent
-            const bool whole = (t0 + kSub - 1 <= seen_by_all && pos_last - t0 < window) || t0 + kSub <= rq.r.pre;
-            if (whole && !p.slopes) {
+        int it = 0;
+        do {  // a loop of its own for what the tensor core adds up: the rare rest costs the steps no registers
+            do {
+                copy_wait<kStages - 2>();
+                store_exp();
+                __syncwarp();  // the entry has landed for every lane, and the one before it has been read by all
+                fetch(it + kStages - 1);
+
+                const int st = it % kStages, t0 = tile_tok(it);
+                const uint8_t* ks = sm.ring[st][0];
+                const uint8_t* vs = sm.ring[st][1];
+                const float kf[2] = {exp2i(sm.exps[st][0][0]), exp2i(sm.exps[st][0][1])};
+                const int ve[2] = {sm.exps[st][1][0], sm.exps[st][1][1]};
+
+                // S^T[16 tokens][block of rows]: element e is token 16 j + 8 (e / 2) + qr, row 2 qc + e % 2
+                float s[2][NB][4];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int i = 0; i < NR; ++i) {
-                        const float a = fminf(rs[i] * kf[j], 3.0e38f);
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float& x = s[j][i >> 1][2 * e + (i & 1)];
-                            if (p.cap2 > 0.0f) x = capped<CAP>(x * a, p.cap2, cap_in) + (float)ve[j];
-                            else x = fmaf(x, a, (float)ve[j]);
+                        for (int e = 0; e < 4; ++e) s[j][nb][e] = 0.0f;
+#pragma unroll
+                for (int hh = 0; hh < D / 64; ++hh) {
+                    uint32_t kw[4][4];  // rows 8 j + qr
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(ks + chunk_off<D>(8 * j + qr, qc + 4 * hh));
+                        kw[j][0] = w.x, kw[j][1] = w.y, kw[j][2] = w.z, kw[j][3] = w.w;
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        uint2 b[kParts][NB];
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+                                b[part][nb] = *reinterpret_cast<const uint2*>(sm.q[part][nb][hh][kk][lane]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t w0 = kw[2 * j][kk], w1 = kw[2 * j + 1][kk];
+                            const uint32_t a[4] = {widen_lo(w0), widen_lo(w1), widen_hi(w0), widen_hi(w1)};
+#pragma unroll
+                            for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                                for (int nb = 0; nb < NB; ++nb) mma16816(s[j][nb], a, b[part][nb].x, b[part][nb].y);
                         }
                     }
-            } else {
+                }
+
+                // scores in base-2 units plus the value exponent
+                const bool whole = (t0 + kSub - 1 <= seen_by_all && pos_last - t0 < window) || t0 + kSub <= rq.r.pre;
+                if (whole && !p.slopes) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int t = t0 + 16 * j + 8 * e + qr;
-                        int at = t, draft = -1;  // the token's position, and which draft of a tree it is
-                        if (p.parents && t >= rq.base) {
-                            draft = min(t - rq.base, rq.L - 1);
-                            at = rq.base + sm.depth[draft];
-                        }
-                        const bool always = t < prefix;
+                    for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int i = 0; i < NR; ++i) {
-                            float& x = s[j][i >> 1][2 * e + (i & 1)];
                             const float a = fminf(rs[i] * kf[j], 3.0e38f);
-                            if (modified) {
-                                x *= a;
-                                if (p.cap2 > 0.0f) x = capped<CAP>(x, p.cap2, cap_in);
-                                x = fmaf(-slope[i], fabsf((float)(pos[i] - at)), x) + (float)ve[j];
-                            } else {
-                                x = fmaf(x, a, (float)ve[j]);  // as above: a mask changes no bit of what is seen
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float& x = s[j][i >> 1][2 * e + (i & 1)];
+                                if (p.cap2 > 0.0f) x = capped<CAP>(x * a, p.cap2, cap_in) + (float)ve[j];
+                                else x = fmaf(x, a, (float)ve[j]);
                             }
-                            bool sees = draft >= 0 ? (anc[i] >> draft) & 1 : t <= pos[i];
-                            sees = ((sees && pos[i] - at < window) || always) && t < rq.kv;
-                            x = sees ? x : -INFINITY;
                         }
-                    }
-            }
-            float mx[NR];
-            bool move = false;
+                } else {
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                mx[i] = max3(fmaxf(s[0][i >> 1][i & 1], s[0][i >> 1][2 + (i & 1)]), s[1][i >> 1][i & 1], s[1][i >> 1][2 + (i & 1)]);
+                    for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], d));
-                move = move || mx[i] > m[i] + kMaxWeight;
-            }
-            if (__any_sync(0xffffffffu, move)) {
+                        for (int e = 0; e < 2; ++e) {
+                            const int t = t0 + 16 * j + 8 * e + qr;
+                            int at = t, draft = -1;  // the token's position, and which draft of a tree it is
+                            if (p.parents && t >= rq.base) {
+                                draft = min(t - rq.base, rq.L - 1);
+                                at = rq.base + sm.depth[draft];
+                            }
+                            const bool always = t < prefix;
+#pragma unroll
+                            for (int i = 0; i < NR; ++i) {
+                                float& x = s[j][i >> 1][2 * e + (i & 1)];
+                                const float a = fminf(rs[i] * kf[j], 3.0e38f);
+                                if (modified) {
+                                    x *= a;
+                                    if (p.cap2 > 0.0f) x = capped<CAP>(x, p.cap2, cap_in);
+                                    x = fmaf(-slope[i], fabsf((float)(pos[i] - at)), x) + (float)ve[j];
+                                } else {
+                                    x = fmaf(x, a, (float)ve[j]);  // as above: a mask changes no bit of what is seen
+                                }
+                                bool sees = draft >= 0 ? (anc[i] >> draft) & 1 : t <= pos[i];
+                                sees = ((sees && pos[i] - at < window) || always) && t < rq.kv;
+                                x = sees ? x : -INFINITY;
+                            }
+                        }
+                }
+                float mx[NR];
+                bool move = false;
 #pragma unroll
                 for (int i = 0; i < NR; ++i) {
-                    if (mx[i] > m[i] + kMaxWeight) {
-                        const float f = tc::ex2_approx(m[i] - (mx[i] - lift<F32>()));  // 0 from m = -inf
-                        m[i] = mx[i] - lift<F32>();
-                        l[i] *= f;
+                    mx[i] = max3(fmaxf(s[0][i >> 1][i & 1], s[0][i >> 1][2 + (i & 1)]), s[1][i >> 1][i & 1], s[1][i >> 1][2 + (i & 1)]);
 #pragma unroll
-                        for (int d = 0; d < kDT; ++d) {
-                            o[i >> 1][d][i & 1] *= f;
-                            o[i >> 1][d][2 + (i & 1)] *= f;
+                    for (int d = 4; d < 32; d <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], d));
+                    move = move || mx[i] > m[i] + kMaxWeight;
+                }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) {
+                        if (mx[i] > m[i] + kMaxWeight) {
+                            const float f = tc::ex2_approx(m[i] - (mx[i] - lift<F32>()));  // 0 from m = -inf
+                            m[i] = mx[i] - lift<F32>();
+                            l[i] *= f;
+#pragma unroll
+                            for (int d = 0; d < kDT; ++d) {
+                                o[i >> 1][d][i & 1] *= f;
+                                o[i >> 1][d][2 + (i & 1)] *= f;
+                            }
                         }
                     }
                 }
-            }
-            // weights; a row that has seen nothing keeps m = -inf and takes 0 as its reference
-            const float vf[2] = {exp2i(-ve[0]), exp2i(-ve[1])};
+                // weights; a row that has seen nothing keeps m = -inf and takes 0 as its reference
+                const float vf[2] = {exp2i(-ve[0]), exp2i(-ve[1])};
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                const float ref = m[i] == -INFINITY ? 0.0f : m[i];
+                for (int i = 0; i < NR; ++i) {
+                    const float ref = m[i] == -INFINITY ? 0.0f : m[i];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float& x0 = s[j][i >> 1][i & 1];
+                        float& x1 = s[j][i >> 1][2 + (i & 1)];
+                        x0 = tc::ex2_approx(x0 - ref);
+                        x1 = tc::ex2_approx(x1 - ref);
+                        l[i] = fmaf(x0 + x1, vf[j], l[i]);
+                    }
+                }
+
+                // O^T += V^T P^T, 16 tokens at a time
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float& x0 = s[j][i >> 1][i & 1];
-                    float& x1 = s[j][i >> 1][2 + (i & 1)];
-                    x0 = tc::ex2_approx(x0 - ref);
-                    x1 = tc::ex2_approx(x1 - ref);
-                    l[i] = fmaf(x0 + x1, vf[j], l[i]);
-                }
-            }
-
-            // O^T += V^T P^T, 16 tokens at a time
+                    uint32_t b[kParts][NB][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t b[kParts][NB][2];
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
+                        for (int e = 0; e < 2; ++e) {
+                            const float x0 = s[j][nb][2 * e], x1 = s[j][nb][2 * e + 1];
+                            const uint32_t w = tc::pack_f16(x0, x1);
+                            b[0][nb][e] = transpose8x8(w);
+                            if constexpr (F32) {
+                                const float2 r = tc::unpack_f16(w);
+                                b[kParts - 1][nb][e] = transpose8x8(tc::pack_f16(x0 - r.x, x1 - r.y));
+                            }
+                        }
+                    constexpr int kW = D / 32;  // words of a lane's D/8 dimensions of one token
+                    uint32_t w[4][kW];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float x0 = s[j][nb][2 * e], x1 = s[j][nb][2 * e + 1];
-                        const uint32_t w = tc::pack_f16(x0, x1);
-                        b[0][nb][e] = transpose8x8(w);
-                        if constexpr (F32) {
-                            const float2 r = tc::unpack_f16(w);
-                            b[kParts - 1][nb][e] = transpose8x8(tc::pack_f16(x0 - r.x, x1 - r.y));
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 16 * j + 2 * qc + (i & 1) + 8 * (i >> 1);
+                        if constexpr (D == 128) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(vs + chunk_off<D>(r, qr));
+                            w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2*>(vs + chunk_off<D>(r, qr >> 1) + (qr & 1) * 8);
+                            w[i][0] = x.x, w[i][1] = x.y;
                         }
                     }
-                constexpr int kW = D / 32;  // words of a lane's D/8 dimensions of one token
-                uint32_t w[4][kW];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * j + 2 * qc + (i & 1) + 8 * (i >> 1);
-                    if constexpr (D == 128) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(vs + chunk_off<D>(r, qr));
-                        w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
-                    } else {
-                        const uint2 x = *reinterpret_cast<const uint2*>(vs + chunk_off<D>(r, qr >> 1) + (qr & 1) * 8);
-                        w[i][0] = x.x, w[i][1] = x.y;
-                    }
+                    for (int x = 0; x < kW; ++x)
+#pragma unroll
+                        for (int d = 0; d < 2; ++d) {
+                            // bytes 2 d and 2 d + 1 of two tokens interleaved: dimensions 4 x + 2 d and the next are the row
+                            // tile's rows qr and qr + 8
+                            const uint32_t lo = __byte_perm(w[0][x], w[1][x], d ? 0x7362 : 0x5140);
+                            const uint32_t hi = __byte_perm(w[2][x], w[3][x], d ? 0x7362 : 0x5140);
+                            const uint32_t a[4] = {widen_lo(lo), widen_hi(lo), widen_lo(hi), widen_hi(hi)};
+#pragma unroll
+                            for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                                for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][2 * x + d], a, b[part][nb][0], b[part][nb][1]);
+                        }
                 }
-#pragma unroll
-                for (int x = 0; x < kW; ++x)
-#pragma unroll
-                    for (int d = 0; d < 2; ++d) {
-                        // bytes 2 d and 2 d + 1 of two tokens interleaved: dimensions 4 x + 2 d and the next are the row
-                        // tile's rows qr and qr + 8
-                        const uint32_t lo = __byte_perm(w[0][x], w[1][x], d ? 0x7362 : 0x5140);
-                        const uint32_t hi = __byte_perm(w[2][x], w[3][x], d ? 0x7362 : 0x5140);
-                        const uint32_t a[4] = {widen_lo(lo), widen_hi(lo), widen_lo(hi), widen_hi(hi)};
-#pragma unroll
-                        for (int part = 0; part < kParts; ++part)
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][2 * x + d], a, b[part][nb][0], b[part][nb][1]);
-                    }
-            }
-        }
+            } while (++it < steps && it % kFold != 0);
+            if (steps > kFold) fold(it > kFold, it < steps);
+        } while (it < steps);
         copy_wait<0>();
 
         // ---- results: a lane holds D/8 consecutive dimensions of each of its rows
         const bool complete = k0 == 0 && k1 == rq.tiles;
-        const long long slot = (long long)(worker * 2 + (k0 == 0 ? 1 : 0)) * kRows;
+        const long long slot = slot_of();
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
 #pragma unroll

@@ -35,7 +35,8 @@
  *
  * Arithmetic.  Queries are scaled per row by a power of two and rounded to fp16 (exact for bf16 queries
  * down to 2^-28 of the row's largest; for fp32 queries a second fp16 takes the remainder), codes are
- * exact in fp16, products accumulate in fp32, the softmax statistics are fp32, weights are rounded to
+ * exact in fp16, products accumulate in fp32 (on the tensor core, whose additions truncate, over at most 512 tokens for
+ * fp32, 32768 for bf16; those sums are added up with rounding), the softmax statistics are fp32, weights are rounded to
  * fp16 (for fp32 a second fp16 takes their remainder), the output is rounded once to the dtype.  A token's
  * weight times its value page's scale keeps all those bits down to 2^-14 (fp32: 2^-26) of the largest such
  * product of its row; below that it is off by at most 2^-25 (2^-37) of that product.
