@@ -17,8 +17,10 @@
 // tile against 2 x 128 x 128 exponentials, which at 16 a clock and SM take as long as the products at D = 128.
 // Scores are kept in base-2 units; scales, the running reference and the weights are those of attn_split.cu.
 // For fp32 the queries and the weights are two fp16 each (one stream, two products for each one), and O is added up in
-// fp32 instructions every kFold tiles (in the idle stream's columns): the tensor core's own additions
-// truncate, which over hundreds of tiles would cost more than fp32's rounding (3e-6 over 5000 tokens).
+// fp32 instructions every 4 tiles (in the idle stream's columns): the tensor core's own additions
+// truncate, which over hundreds of tiles would cost more than fp32's rounding (3e-6 over 5000 tokens).  bf16 does so every
+// 256 tiles, through global memory: behind a million tokens its outputs had shrunk by 0.29 %, more than their rounding (now
+// 0.01 %; 2 % of the time of such calls, and of capped ones, is what the code for it takes).
 //
 // An item with at most 128 rows (the end of a sequence, a verify pass) has both streams work on the same rows, one
 // on the even and one on the odd tiles ("twin"); stream 0 joins the two results in the end: rows r of both lie in the
@@ -47,7 +49,9 @@ constexpr int kThreads = 16 * 32;
 // registers a thread: 512 x 128 at launch, shared out anew between the softmax and the other warps
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 4 * 128, "more registers than the block is launched with");
-constexpr int kFold = 4;     // fp32: tiles whose values the tensor core adds up
+// Tiles whose values the tensor core adds up at a time (8 additions each, 16 for fp32): its additions truncate (see
+// attn_split.cu).  bf16: at 64 tiles the sums set aside cost extend_long's items of 64 to 128 tiles 5 %.
+template <bool F32> constexpr int fold_tiles() { return F32 ? 4 : 256; }
 constexpr int kExpSlots = 4; // tiles whose exponents are held
 constexpr int kGrid = kSMs;
 
@@ -335,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int kRows = item_rows<F32>();
     constexpr int kSteps = D / 16;  // k-steps of Q K^T
+    constexpr int kFold = fold_tiles<F32>();
     constexpr uint32_t kIdS = tc::idesc_f16(128, kTile), kIdO = tc::idesc_f16(128, D) | tc::kTransposeB;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem<D, kRows>& sm = *reinterpret_cast<Smem<D, kRows>*>(smem_raw);
@@ -448,15 +453,49 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sm.qfull[st]));
             return p.scale2 * exp2i(eq);
         };
+        // bf16: adds the row's sums to what has been set aside of them, if anything, where the row's partial result goes in the
+        // end: there (keep), or in tensor memory.
+        auto set_aside = [&](const Segment& s, float m, bool any, bool keep) {
+            const long long row = (long long)(blockIdx.x * 2 + (s.first ? 1 : 0)) * kRows + tid;
+            const float mf = any ? p.part_ml[row].x : 0.0f, f = mf == -INFINITY ? 0.0f : tc::ex2_approx(mf - m);
+            float4* at = reinterpret_cast<float4*>(p.part_o + row * D);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16, at += 4) {
+                float o[16];
+                float4 y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = any ? at[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+                tc::tmem_ld16(tO + c, o);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[4 * i] = fmaf(y[i].x, f, o[4 * i]), o[4 * i + 1] = fmaf(y[i].y, f, o[4 * i + 1]);
+                    o[4 * i + 2] = fmaf(y[i].z, f, o[4 * i + 2]), o[4 * i + 3] = fmaf(y[i].w, f, o[4 * i + 3]);
+                }
+                if (keep) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) at[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                } else {
+                    uint32_t b[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(o[i]);
+                    tc::tmem_st16(tO + c, b);
+                }
+            }
+            if (keep) p.part_ml[row].x = m;
+            else tc::tmem_st_wait();
+        };
         // The segment's results: outputs of a whole item, a partial result otherwise.
         auto put = [&](const Segment& s, float m, float l) {
             const int row = s.twin ? r : tid, rr = s.rb * kRows + row, t = p.token_of(rr), hq = s.h * p.G + rr - t * p.G;
             const bool any = s.nt[st] > 0;
+            if (!F32 && s.nt[st] > kFold) set_aside(s, m, true, false);
             // Twin streams: rows r of both lie in the same lanes of tensor memory, so that stream 0 reads both accumulators.
             const bool join = s.twin && s.nt[1] > 0;
             float f = 1.0f, f1 = 0.0f;  // of this stream's and the other one's part of the row
             if (join && st == 1) {
                 sm.twin_ml[r] = make_float2(m, l);
+                tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sm.tfull));
                 owed = true;  // stream 0's reading, before the next products of this stream
@@ -580,163 +619,172 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                 const float slope = p.slopes ? p.slopes[hq] * kLog2e : 0.0f;
                 const float cap2 = p.cap2, cap_in = CAP != kNoCap ? 2.0f * kLog2e / cap2 : 0.0f;
 
-                for (int j = 0; j < nt && ok; ++j) {
-                    const int i = s.twin ? 2 * j + st : j, k = k0 + i, t0 = (k < ta ? k : k + skip) * kTile, es = (tile + i) % kExpSlots;
-                    ok = tc::mbar_wait(tc::smem_u32(&sm.sfull[st]), n_s & 1);
-                    ++n_s;
-                    tc::fence_after_sync();
-                    // every row of the stream sees the whole tile, and no bias depends on the place
-                    const bool whole = !p.slopes && ((t0 + kTile - 1 <= pos_first && (p.window <= 0 || pos_last - t0 < p.window)) ||
-                                                     t0 + kTile <= s.t.pre);
-                    const uint32_t scales = tc::smem_u32(sm.scale[es]);
-                    // read where they are used, each time (kept in registers they would make the scores spill)
-                    auto scale = [&](int g) {
-                        float4 f;
-                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                     : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-                                     : "r"(scales + g * 16));
-                        f.x = fmaxf(1.0e-37f, fminf(rs * f.x, 3.0e38f));  // a masked score, -inf, stays that
-                        return f;
-                    };
-                    const bool plain = CAP == kNoCap && !p.slopes;  // scores are only scaled, below; otherwise the scale below is 1
-                    if (!whole) {
-                        // Mask (unless plain: scale, cap and bias too) in tensor memory, 16 columns at a time, in loops of
-                        // their own: unrolled over the registers below they would double the loop's code.
-                        auto rewrite = [&](auto edit) {
-#pragma unroll 1
-                            for (int g = 0; g < kTile / 16; ++g) {
-                                float y[16];
-                                uint32_t b[16];
-                                tc::tmem_ld16(tS + g * 16, y);
-                                const float a = scale(g).x;
-                                tc::tmem_ld_wait();
-                                if constexpr (CAP != kNoCap) cap16<CAP>(y, a, cap2, cap_in);
-                                if (CAP == kNoCap && !plain)
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) y[i] *= a;
-                                edit(y, t0 + g * 16);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(y[i]);
-                                tc::tmem_st16(tS + g * 16, b);
-                            }
-                            tc::tmem_st_wait();
+                int j = 0;
+                do {  // (a loop of its own for what is added up before it is set aside)
+                    do {
+                        const int i = s.twin ? 2 * j + st : j, k = k0 + i, t0 = (k < ta ? k : k + skip) * kTile, es = (tile + i) % kExpSlots;
+                        ok = tc::mbar_wait(tc::smem_u32(&sm.sfull[st]), n_s & 1);
+                        ++n_s;
+                        tc::fence_after_sync();
+                        // every row of the stream sees the whole tile, and no bias depends on the place
+                        const bool whole = !p.slopes && ((t0 + kTile - 1 <= pos_first && (p.window <= 0 || pos_last - t0 < p.window)) ||
+                                                         t0 + kTile <= s.t.pre);
+                        const uint32_t scales = tc::smem_u32(sm.scale[es]);
+                        // read where they are used, each time (kept in registers they would make the scores spill)
+                        auto scale = [&](int g) {
+                            float4 f;
+                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                         : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                                         : "r"(scales + g * 16));
+                            f.x = fmaxf(1.0e-37f, fminf(rs * f.x, 3.0e38f));  // a masked score, -inf, stays that
+                            return f;
                         };
-                        auto sees = [&](int tok) { return (uint32_t)(tok - vlo) < (uint32_t)(vhi - vlo) || tok < pre; };
-                        auto biased = [&](float y, int at) { return fmaf(-slope, fabsf((float)(pos - at)), y); };
-                        if (!p.slopes && !p.parents) {
-                            rewrite([&](float* y, int tok) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) y[i] = sees(tok + i) ? y[i] : -INFINITY;
-                            });
-                        } else {
-                            rewrite([&](float* y, int tok) {
-                                if (p.parents && tok + 16 > s.g.base && tok < s.g.kv) {  // drafts of a tree among the tokens
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) {
-                                        const int d = max(0, min(tok + i - s.g.base, s.g.L - 1));
-                                        const int at = tok + i < s.g.base ? tok + i : s.g.base + tree.depth[d];
-                                        const bool seen = tok + i < s.g.base ? sees(tok + i)
-                                                                             : (((anc >> d) & 1) && at >= vlo && tok + i < s.g.kv) || tok + i < pre;
-                                        y[i] = seen ? (p.slopes ? biased(y[i], at) : y[i]) : -INFINITY;
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        y[i] = sees(tok + i) ? (p.slopes ? biased(y[i], tok + i) : y[i]) : -INFINITY;
-                                }
-                            });
-                        }
-                    }
-                    float x[kTile];
-#pragma unroll
-                    for (int c = 0; c < kTile; c += 32) tmem_ld32(tS + c, x + c);
-                    tc::tmem_ld_wait();
-                    if constexpr (CAP != kNoCap) {  // scaled and capped here; below the scale is 1
-                        if (whole)
-#pragma unroll
-                            for (int g = 0; g < kTile / 16; ++g) cap16<CAP>(x + g * 16, scale(g).x, cap2, cap_in);
-                    }
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int g = 0; g < kTile / 16; ++g) {
-                        const float* y = x + g * 16;
-                        const float m0 = max3(y[0], y[1], y[2]), m1 = max3(y[3], y[4], y[5]), m2 = max3(y[6], y[7], y[8]),
-                                    m3 = max3(y[9], y[10], y[11]), m4 = max3(y[12], y[13], y[14]);
-                        const float4 f = scale(g);
-                        mx = fmaxf(mx, fmaf(fmaxf(max3(m0, m1, m2), max3(m3, m4, y[15])), plain ? f.x : 1.0f, f.y));
-                    }
-                    auto for_output = [&](uint32_t cols, float f) {  // scales 32 lanes of an accumulator
+                        const bool plain = CAP == kNoCap && !p.slopes;  // scores are only scaled, below; otherwise the scale below is 1
+                        if (!whole) {
+                            // Mask (unless plain: scale, cap and bias too) in tensor memory, 16 columns at a time, in loops of
+                            // their own: unrolled over the registers below they would double the loop's code.
+                            auto rewrite = [&](auto edit) {
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            float o[16];
-                            uint32_t b[16];
-                            tc::tmem_ld16(cols + c, o);
-                            tc::tmem_ld_wait();
+                                for (int g = 0; g < kTile / 16; ++g) {
+                                    float y[16];
+                                    uint32_t b[16];
+                                    tc::tmem_ld16(tS + g * 16, y);
+                                    const float a = scale(g).x;
+                                    tc::tmem_ld_wait();
+                                    if constexpr (CAP != kNoCap) cap16<CAP>(y, a, cap2, cap_in);
+                                    if (CAP == kNoCap && !plain)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(o[i] * f);
-                            tc::tmem_st16(cols + c, b);
+                                        for (int i = 0; i < 16; ++i) y[i] *= a;
+                                    edit(y, t0 + g * 16);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(y[i]);
+                                    tc::tmem_st16(tS + g * 16, b);
+                                }
+                                tc::tmem_st_wait();
+                            };
+                            auto sees = [&](int tok) { return (uint32_t)(tok - vlo) < (uint32_t)(vhi - vlo) || tok < pre; };
+                            auto biased = [&](float y, int at) { return fmaf(-slope, fabsf((float)(pos - at)), y); };
+                            if (!p.slopes && !p.parents) {
+                                rewrite([&](float* y, int tok) {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) y[i] = sees(tok + i) ? y[i] : -INFINITY;
+                                });
+                            } else {
+                                rewrite([&](float* y, int tok) {
+                                    if (p.parents && tok + 16 > s.g.base && tok < s.g.kv) {  // drafts of a tree among the tokens
+#pragma unroll
+                                        for (int i = 0; i < 16; ++i) {
+                                            const int d = max(0, min(tok + i - s.g.base, s.g.L - 1));
+                                            const int at = tok + i < s.g.base ? tok + i : s.g.base + tree.depth[d];
+                                            const bool seen = tok + i < s.g.base ? sees(tok + i)
+                                                                                 : (((anc >> d) & 1) && at >= vlo && tok + i < s.g.kv) || tok + i < pre;
+                                            y[i] = seen ? (p.slopes ? biased(y[i], at) : y[i]) : -INFINITY;
+                                        }
+                                    } else {
+#pragma unroll
+                                        for (int i = 0; i < 16; ++i)
+                                            y[i] = sees(tok + i) ? (p.slopes ? biased(y[i], tok + i) : y[i]) : -INFINITY;
+                                    }
+                                });
+                            }
                         }
-                    };
-                    if constexpr (F32) {
-                        if (j > 0 && j % kFold == 0) {  // the tensor core starts O anew at this tile
+                        float x[kTile];
+#pragma unroll
+                        for (int c = 0; c < kTile; c += 32) tmem_ld32(tS + c, x + c);
+                        tc::tmem_ld_wait();
+                        if constexpr (CAP != kNoCap) {  // scaled and capped here; below the scale is 1
+                            if (whole)
+#pragma unroll
+                                for (int g = 0; g < kTile / 16; ++g) cap16<CAP>(x + g * 16, scale(g).x, cap2, cap_in);
+                        }
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int g = 0; g < kTile / 16; ++g) {
+                            const float* y = x + g * 16;
+                            const float m0 = max3(y[0], y[1], y[2]), m1 = max3(y[3], y[4], y[5]), m2 = max3(y[6], y[7], y[8]),
+                                        m3 = max3(y[9], y[10], y[11]), m4 = max3(y[12], y[13], y[14]);
+                            const float4 f = scale(g);
+                            mx = fmaxf(mx, fmaf(fmaxf(max3(m0, m1, m2), max3(m3, m4, y[15])), plain ? f.x : 1.0f, f.y));
+                        }
+                        auto for_output = [&](uint32_t cols, float f) {  // scales 32 lanes of an accumulator
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
-                                float o[16], sum[16];
+                                float o[16];
                                 uint32_t b[16];
-                                tc::tmem_ld16(tO + c, o);
-                                tc::tmem_ld16(tSum + c, sum);
+                                tc::tmem_ld16(cols + c, o);
                                 tc::tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(j == kFold ? o[i] : o[i] + sum[i]);
-                                tc::tmem_st16(tSum + c, b);
+                                for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(o[i] * f);
+                                tc::tmem_st16(cols + c, b);
                             }
-                            tc::tmem_st_wait();
-                        }
-                    }
-                    const bool move = mx > m + kMaxWeight;
-                    if (__any_sync(0xffffffffu, move)) {
-                        float fo = 1.0f;
-                        if (move) {
-                            fo = tc::ex2_approx(m - (mx - lift<F32>()));  // 0 from m = -inf
-                            m = mx - lift<F32>();
-                            l *= fo;
-                        }
-                        if (F32 ? j % kFold != 0 : j > 0) for_output(tO, fo);
-                        if (F32 && j >= kFold) for_output(tSum, fo);
-                    }
-                    if (owed) {
-                        ok = ok && tc::mbar_wait(tc::smem_u32(&sm.tempty), n_t++ & 1);
-                        owed = false;
-                    }
-                    const float ref = m == -INFINITY ? 0.0f : m;
+                        };
+                        if constexpr (F32) {
+                            if (j > 0 && j % kFold == 0) {  // the tensor core starts O anew at this tile
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 16) {
+                                    float o[16], sum[16];
+                                    uint32_t b[16];
+                                    tc::tmem_ld16(tO + c, o);
+                                    tc::tmem_ld16(tSum + c, sum);
+                                    tc::tmem_ld_wait();
 #pragma unroll
-                    for (int g = 0; g < kTile / 16; ++g) {
-                        const float4 f = scale(g);
-                        const float a = plain ? f.x : 1.0f, off = f.y - ref;
-                        float* y = x + g * 16;
-                        float s0 = 0.0f, s1 = 0.0f;
-                        uint32_t hi[8], lo[8];
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            fma2(y[i], y[i + 1], a, off);
-                            y[i] = tc::ex2_approx(y[i]);
-                            y[i + 1] = tc::ex2_approx(y[i + 1]);
-                            add2(s0, s1, y[i], y[i + 1]);
-                            hi[i / 2] = tc::pack_f16(y[i], y[i + 1]);
-                            if constexpr (F32) {
-                                const float2 b = tc::unpack_f16(hi[i / 2]);
-                                lo[i / 2] = tc::pack_f16(y[i] - b.x, y[i + 1] - b.y);
+                                    for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(j == kFold ? o[i] : o[i] + sum[i]);
+                                    tc::tmem_st16(tSum + c, b);
+                                }
+                                tc::tmem_st_wait();
                             }
                         }
-                        l = fmaf(s0 + s1, f.z, l);
-                        tc::tmem_st8(tP + g * 8, hi);  // in place of the scores (fp32: in the idle stream's columns)
-                        if constexpr (F32) tc::tmem_st8(tP + 64 + g * 8, lo);
+                        const bool move = mx > m + kMaxWeight;
+                        if (__any_sync(0xffffffffu, move)) {
+                            float fo = 1.0f;
+                            if (move) {
+                                fo = tc::ex2_approx(m - (mx - lift<F32>()));  // 0 from m = -inf
+                                m = mx - lift<F32>();
+                                l *= fo;
+                            }
+                            if (j % kFold != 0) for_output(tO, fo);
+                            if (F32 && j >= kFold) for_output(tSum, fo);
+                        }
+                        if (owed) {
+                            ok = ok && tc::mbar_wait(tc::smem_u32(&sm.tempty), n_t++ & 1);
+                            owed = false;
+                        }
+                        const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                        for (int g = 0; g < kTile / 16; ++g) {
+                            const float4 f = scale(g);
+                            const float a = plain ? f.x : 1.0f, off = f.y - ref;
+                            float* y = x + g * 16;
+                            float s0 = 0.0f, s1 = 0.0f;
+                            uint32_t hi[8], lo[8];
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                fma2(y[i], y[i + 1], a, off);
+                                y[i] = tc::ex2_approx(y[i]);
+                                y[i + 1] = tc::ex2_approx(y[i + 1]);
+                                add2(s0, s1, y[i], y[i + 1]);
+                                hi[i / 2] = tc::pack_f16(y[i], y[i + 1]);
+                                if constexpr (F32) {
+                                    const float2 b = tc::unpack_f16(hi[i / 2]);
+                                    lo[i / 2] = tc::pack_f16(y[i] - b.x, y[i + 1] - b.y);
+                                }
+                            }
+                            l = fmaf(s0 + s1, f.z, l);
+                            tc::tmem_st8(tP + g * 8, hi);  // in place of the scores (fp32: in the idle stream's columns)
+                            if constexpr (F32) tc::tmem_st8(tP + 64 + g * 8, lo);
+                        }
+                        tc::tmem_st_wait();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sm.pfull[st]));
+                    } while (++j < nt && ok && (F32 || j % kFold != 0));
+                    if (!F32 && j < nt && ok) {  // with the next scores the products before them have completed
+                        ok = tc::mbar_wait(tc::smem_u32(&sm.sfull[st]), n_s & 1);
+                        tc::fence_after_sync();
+                        set_aside(s, m, j > kFold, true);
+                        tc::fence_before_sync();
                     }
-                    tc::tmem_st_wait();
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sm.pfull[st]));
-                }
+                } while (j < nt && ok);
             }
             tile += s.steps;
         }
@@ -919,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                     tc::fence_after_sync();
                     if (lane == 0) {
                         if (pv) {
-                            values(st, g & 1, F32 ? j % kFold != 0 : j > 0);
+                            values(st, g & 1, j % kFold != 0);
                             if (last) tc::mma_commit(tc::smem_u32(&sm.vempty[g & 1]));
                         }
                         if (qk) {

@@ -93,3 +93,33 @@ def test_short_items_around_the_length_that_is_added_up_at_once(dtype, rows, G):
     out = torch.cat([out[i * rows:(i + 1) * rows] for i in some])
     s.kv = [kv[i] for i in some]
     check_all(s, out)
+
+
+def shrink(s, out, picks):
+    """The mean relative error of some rows, in the standard deviations of its rounding too."""
+    rel = torch.cat([((out[i * s.rows + r].double() - x) / x).flatten() for i, r in picks for x in [s.want(i, r)]])
+    return rel.mean().item(), 2.0 ** -8 / math.sqrt(3 * rel.numel())
+
+
+@pytest.mark.parametrize("n,rows,G,kv", [(1, 40960, 1, 524288 + 40960),  # items of 256 rows
+                                         (300, 1, 40, 524288)])         # of 40, whose tiles two streams share
+def test_bf16_sums_keep_their_size(n, rows, G, kv):
+    """The roundings of many outputs cancel; what is left is the shrinking (0.13 % where 524288 tokens are one sum)."""
+    s = Shared(rows, [kv] * n, G, BF, spread=2.5, seed=5)
+    out = s.run()
+    picks = [(7 * i % n, 641 * i % rows) for i in range(64)]
+    mean, sigma = shrink(s, out, picks)
+    assert abs(mean) <= 2048 * 2.0 ** -23 + 5 * sigma, mean
+
+
+@pytest.mark.parametrize("G,rows,unit", [(1, 256, 32768), (40, 1, 65536), (3, 100, 32768)])
+def test_items_around_the_tiles_that_are_added_up_at_once(G, rows, unit):
+    """One item or two of 256 rows, or one of 40, per request, of 255 to 513 tiles a stream."""
+    kv = [unit * (1 + i % 2) + (0, 1, 127, 128, 129, -1, -128, 300)[i % 8] for i in range(170)]
+    s = Shared(rows, kv, G, BF, seed=6)
+    out = s.run()
+    picks = [(i, r) for i in range(0, 170, 3) for r in (0, rows // 2, rows - 1)]
+    for i, r in picks:
+        ref = s.want(i, r)
+        worst = ((out[i * rows + r].double() - ref).abs() / ref).max().item()
+        assert worst <= 2.0 ** -8 + 2.0 ** -11 + SCORES + 2048 * 2.0 ** -23, (i, r, kv[i], worst)
