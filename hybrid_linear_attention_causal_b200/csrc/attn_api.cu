@@ -71,20 +71,13 @@ struct Call {
     gdn_stream_t stream;
 };
 
-// The kernel of 128-row tensor-core tiles takes the same time for 8 rows per key as for 128; the split kernel reads the cache
-// once for every 32 rows, so it is the faster one up to there.  Measured (B200, us, split / tiles; 64 requests of 500 to
-// 8000 tokens, 32/8 heads of 128): 8 rows per key 77 / 209, 16: 92 / 210, 24: 164 / 210, 32: 174 / 210, 40: 285 / 211,
-// 48: 291 / 211; 2 key heads, 16 to 48 rows: 58, 98, 104, 161, 163 / 104 to 108; heads of 64, 32 and 40 rows: 109 / 173, 175 / 170;
-// fp32, 16, 32 and 40 rows: 114 / 301, 335 / 305, 611 / 302.
-constexpr int kSplitRows = 32;
-
 // How a call's requests are shared out between the two: by their average, which for a ragged batch says nothing of any one
 // of them.  From 2048 rows above one token per request (64 more passes over a cache, if one request has them), each goes to
 // the kernel that its own rows ask for, at the price of three more launches: 256 requests of 2 rows, 16/2 heads, 107 us (all in
 // tiles 190, as drafts to verify 91); 255 single rows and one request of 600 behind 8000 tokens, 32/8 heads, 384 us (788).
 enum Kernels { kSplit, kTiles, kBoth };
-Kernels kernels_for(const int32_t* cu, int64_t N, int64_t T, int64_t G) {
-    if (T * G > kSplitRows * N) return kTiles;
+Kernels kernels_for(const int32_t* cu, int64_t N, int64_t T, int64_t G, int split_rows) {
+    if (T * G > split_rows * N) return kTiles;
     return cu && (T - N) * G >= 2048 ? kBoth : kSplit;
 }
 
@@ -140,8 +133,9 @@ int attend(const Call& c) {
     a.hdr = static_cast<int32_t*>(c.ws);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(c.stream);
     gdn::mark_launch(s, 0);
-    const Kernels kernels = kernels_for(c.cu, c.N, c.T, G);
-    a.rows_upto = a.rows_above = kernels == kBoth ? kSplitRows : kernels == kTiles ? 0 : INT32_MAX;
+    const int split_rows = gdn::attn::split_rows(D, c.cfg->dtype == GDN_DTYPE_F32);
+    const Kernels kernels = kernels_for(c.cu, c.N, c.T, G, split_rows);
+    a.rows_upto = a.rows_above = kernels == kBoth ? split_rows : kernels == kTiles ? 0 : INT32_MAX;
     cudaError_t e = cudaSuccess;
     if (kernels != kTiles) e = gdn::attn::launch_split(a, D, c.cfg->dtype, s);
     if (kernels != kSplit && e == cudaSuccess) e = gdn::attn::launch_extend_tc(a, D, c.cfg->dtype, s);

@@ -202,6 +202,14 @@ template <Cap CAP> __device__ __forceinline__ float capped(float x, float cap2, 
 
 cudaError_t launch_append(const AppendArgs& a, int head_dim, int dtype, cudaStream_t s);
 
+// The rows per key up to which the split kernel is the faster one.  The kernel of 128-row tensor-core tiles takes the same time
+// for 8 rows per key as for 128; the split kernel reads the cache once for every 32 rows, and fp32 at D = 128, two parts
+// of each operand, falls behind with the last 16 of them.  Measured (B200, us, split / tiles; 64 requests of 500 to 8000
+// tokens, 32/8 heads of 128): 8 rows per key 77 / 207, 16: 93 / 209, 24: 168 / 210, 32: 179 / 209, 40: 292 / 211, 48: 298 /
+// 210; 2 key heads, 16 to 48 rows: 59, 101, 107, 164, 165 / 104 to 107; heads of 64, 32 and 40 rows: 109, 177 / 173.
+// fp32, 16, 20, 32 and 40 rows: 118, 362, 374, 693 / 302 to 305; heads of 64: 83, 166, 173, 311 / 245.
+constexpr int split_rows(int D, bool F32) { return F32 && D == 128 ? 16 : 32; }
+
 // Attention over the cache, split along the tokens (attn_split.cu): any mode, few rows per key.
 cudaError_t launch_split(Args a, int head_dim, int dtype, cudaStream_t s);
 size_t split_workspace_bytes(int head_dim);

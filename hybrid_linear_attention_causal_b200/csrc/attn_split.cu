@@ -46,7 +46,7 @@ constexpr int kItemSteps = 4;           // steps that beginning and ending an it
 // three blocks instead, of which two fit, had its last third wait for the rest: 64 requests of 64 to 16384 tokens, 32/8
 // heads, 110 us against 84; 4 of 100001 to 131072, 32/4 heads, 131 against 97.
 constexpr int ctas_per_sm(int D, int NB, bool F32) {
-    if (D == 128) return F32 ? (NB == 4 ? 1 : 2) : NB == 1 ? 3 : 2;
+    if (D == 128) return NB == 1 && !F32 ? 3 : 2;
     return NB == 1 ? 4 : NB == 2 ? 3 : 2;
 }
 constexpr int grid_size(int D, int NB, bool F32) { return kSMs * ctas_per_sm(D, NB, F32); }
@@ -55,7 +55,7 @@ constexpr int num_workers(int D, int NB, bool F32) { return grid_size(D, NB, F32
 // Steps that the tensor core adds up at a time.  Its additions truncate, so that a long sum shrinks, by some 2^-25 of itself
 // an addition (64 requests of 131072 tokens, 8 heads of 128: 1.4e-4 in fp32, of 1048576: 1.2e-3): what it holds is added to the
 // warp's partial result in fp32 instructions every 512 tokens for fp32 (64 additions; 9e-7 for either) and every 4096 for
-// bf16 (256; 6e-5).  Time: bf16 0 to 2 %, fp32 5 % (10 % with 32 rows per key).
+// bf16 (256; 6e-5).  Time: bf16 0 to 2 %, fp32 5 %.
 template <bool F32> constexpr int fold_steps() { return F32 ? 16 : 128; }
 
 constexpr int kJoinGrid = 4 * kSMs;
@@ -759,7 +759,9 @@ template <typename T, int D>
 cudaError_t launch_dim(const Args& p, cudaStream_t s) {
     // rows that read each key, in blocks of 8: one, two or four share each widened code
     const long long rows = p.cu ? (long long)p.T * p.G / (p.N > 0 ? p.N : 1) : (long long)p.per * p.G;
-    return rows > 16 ? launch_rows<T, D, 4>(p, s) : rows > 8 ? launch_rows<T, D, 2>(p, s) : launch_rows<T, D, 1>(p, s);
+    if constexpr (split_rows(D, sizeof(T) == 4) > 16)
+        if (rows > 16) return launch_rows<T, D, 4>(p, s);
+    return rows > 8 ? launch_rows<T, D, 2>(p, s) : launch_rows<T, D, 1>(p, s);
 }
 
 size_t round16(size_t x) { return (x + 15) & ~(size_t)15; }
