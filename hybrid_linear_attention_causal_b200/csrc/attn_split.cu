@@ -25,7 +25,7 @@
 //
 // Measured (B200, copy rate 6.55 TB/s): 64 requests of 64 to 16384 tokens, 32/8 heads of 128: 79 us, 5.1 TB/s; 16 rows
 // per key (verify, 4 drafts): 92 us for 363 MB, 3.9 TB/s.  At 8 rows per key a step is about 650 instructions
-// issued at 46 % of the slots: latency is what is left.  Two blocks of rows need 240 registers, so eight warps an SM.
+// issued at 44 % of the slots: latency is what is left.  Two blocks of rows need 240 registers, so eight warps an SM.
 #include <math.h>
 
 #include "attn_internal.cuh"
