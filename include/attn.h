@@ -62,6 +62,8 @@
  * the *_stride arguments give the distance between rows in elements, 0 for contiguous rows; a row's
  * byte distance must be a multiple of 16.  out is contiguous [T, HQ, head_dim].  T * (HQ / HKV) must be below
  * 2^25 (attn_append: T at most 2^30), max_pages * page_size at most 2^30 and N at most 2^28 (GDN_ERR_UNSUPPORTED).
+ * Waits inside the kernels give up after two seconds (GDN_DEVERR_TIMEOUT; results are invalid): rows that read more than
+ * some 5 * 10^7 tokens of one request in one call can take a block that long.
  */
 #ifndef ATTN_H
 #define ATTN_H
