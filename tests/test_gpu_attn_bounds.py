@@ -70,8 +70,9 @@ def test_short_extends_are_verified_drafts(dtype, n, L, hq, hkv):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("opts", [{}, dict(cap=20.0, window=70, slopes=[0.5 / (h + 1) for h in range(8)])])
-def test_long_requests_among_many_short_ones(dtype, opts):
+def test_long_requests_among_many_short_ones(dtype, d, opts):
     """Requests on both sides of the rows at which the kernels change, with padding, lengths too short and too long,
     requests without rows and rows behind the last request among them, on either side."""
     rng = np.random.default_rng(54)
@@ -81,7 +82,7 @@ def test_long_requests_among_many_short_ones(dtype, opts):
         lens[i] = rows
     kv = [int(max(l, x)) for l, x in zip(lens, rng.integers(1, 200, n))]
     kv[150], kv[199], kv[60], kv[52] = 900, 130, 777, 30
-    c = Case(lens, kv, 2 * G, 2, 64, 16, dtype, seed=54)
+    c = Case(lens, kv, 2 * G, 2, d, 16, dtype, seed=54)
     T = sum(lens)
     q = torch.cat([c.q, c.q[:9]]).cuda()
     out = torch.full((T + 9, c.hq, c.d), 7.0, dtype=dtype, device="cuda")
@@ -102,6 +103,14 @@ def test_long_requests_among_many_short_ones(dtype, opts):
     c.kv = [-1 if i in (91, 92, 120) else x for i, x in enumerate(c.kv)]
     check_rows(c, (again[:T], lagain[:T]), **opts)
     assert keep.sum() == T - 97
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("D,G", [(1, 16), (1, 17), (2, 8), (1, 32), (1, 33), (4, 8), (3, 11)])
+def test_rows_per_key_where_the_kernels_change(dtype, d, D, G):
+    c = Case([D] * 5, [300, D, 0, 64, 129], G, 1, d, 32, dtype, seed=58)
+    attend(c, "verify", D)
 
 
 def test_a_mixed_batch_captured():
