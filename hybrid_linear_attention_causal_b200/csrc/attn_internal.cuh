@@ -188,8 +188,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // The two forms of cap * tanh(x / cap), in base-2 units.  kExpCap: cap - 2 cap / (1 + e^(2 x / cap)), cap_in =
 // 2 log2(e) / cap; it is off by up to 2^-20 of the cap however small the score, so it serves bf16 alone, up to kMaxExpCap,
 // where that is less than the weights' rounding to fp16.  kTanhCap: the library's tanh, off by 2^-20 of the score
-// whatever the cap, for fp32 and for larger caps.  Caps 256 and 257 (B200): 12373 rows in a window, 16/4 heads of 128, 320
-// and 507 us; 32 rows per key (64 requests of 500 to 8000 tokens, 8 key heads) 196 and 256 us; 8 rows per key 95.5 and 96.6 us.
+// whatever the cap, for fp32 and for larger caps.  Caps 256 and 257 (B200): 12373 rows in a window, 16/4 heads of 128, 328
+// and 535 us; 32 rows per key (64 requests of 500 to 8000 tokens, 8 key heads) 201 and 263 us; 8 rows per key 96 and 97 us.
 enum Cap { kNoCap, kExpCap, kTanhCap };
 constexpr float kMaxExpCap = 256.0f * kLog2e;
 template <bool F32> inline Cap cap_form(float cap2) {

@@ -44,7 +44,7 @@ constexpr int kItemSteps = 4;           // steps that beginning and ending an it
 // Blocks that an SM holds at a time, by registers and, for fp32's two parts of each query at D = 128, by shared memory
 // (the kernel asserts the latter): the list is cut for exactly the warps that run at once.  fp32 at D = 128 cut for bf16's
 // three blocks instead, of which two fit, had its last third wait for the rest: 64 requests of 64 to 16384 tokens, 32/8
-// heads, 110 us against 84; 4 of 100001 to 131072, 32/4 heads, 131 against 97.
+// heads, 110 us against 84; 4 of 100001 to 131072, 32/4 heads, 131 against 97 (before fold_steps below: now 88 and 102).
 constexpr int ctas_per_sm(int D, int NB, bool F32) {
     if (D == 128) return NB == 1 && !F32 ? 3 : 2;
     return NB == 1 ? 4 : NB == 2 ? 3 : 2;
